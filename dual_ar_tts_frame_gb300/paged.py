@@ -115,21 +115,6 @@ def _on(dev: int):
     return _here if _current() == dev else torch.cuda.device(dev)
 
 
-# Workspaces of calls that bring none: one per device and stream, whose work runs
-# in order.  A call that is being captured gets one of its own, in the graph's pool:
-# the graph may be replayed on any stream.
-_workspaces: dict[tuple[int, int], torch.Tensor] = {}
-
-
-def _workspace(size: int, device: torch.device, stream: int) -> torch.Tensor:
-    if size <= 0 or torch.cuda.is_current_stream_capturing():
-        return torch.empty(max(size, 0), dtype=torch.uint8, device=device)
-    ws = _workspaces.get((device.index, stream))
-    if ws is None or ws.numel() < size:
-        ws = _workspaces[device.index, stream] = torch.empty(size, dtype=torch.uint8, device=device)
-    return ws
-
-
 def kv_page_bytes(n_kv_head: int, head_dim: int, bits: int = 16) -> int:
     """Bytes of one layer of one page."""
     n = L.lib().dualar_kv_page_bytes(n_kv_head, head_dim, bits)
@@ -246,7 +231,7 @@ def paged_attention(q: torch.Tensor, kv: torch.Tensor, table: torch.Tensor, row_
     the row's own; else the last `window` of them and the first `sinks`.  scale:
     head_dim^-0.5 by default.  Rows behind the last request are left as they are
     in `out` (undefined where it is allocated here).  workspace: by default one
-    that is kept per stream (a captured call's own)."""
+    that the call allocates; a given one belongs to one call at a time."""
     c, dev, lib = _kv(kv), kv.get_device(), L.lib()
     d = c.head_dim
     rows, h, dq = q.shape if q.dim() == 3 else (0, 0, 0)
@@ -261,7 +246,6 @@ def paged_attention(q: torch.Tensor, kv: torch.Tensor, table: torch.Tensor, row_
         _bad(f"paged_attention: a table of {nt} rows for {n} requests")
     lens, tab = _i32("kv_len", kv_len, dev), _i32("table", table, dev)
     start = _i32("row_start", row_start, dev, n + 1)
-    stream = _raw_stream(dev)
     with _on(dev):
         if out is None:
             out, ldo = torch.empty((rows, h, d), dtype=q.dtype, device=kv.device), h * d
@@ -269,14 +253,17 @@ def paged_attention(q: torch.Tensor, kv: torch.Tensor, table: torch.Tensor, row_
             ldo = _out(out, q, dev, rows, h, d)
         if workspace is None:
             size = lib.dualar_paged_attention_workspace(act, rows, h, c, n)
-            ws = (workspace := _workspace(size, kv.device, stream)).data_ptr()
+            # this call's own: a call queues two kernels, and another thread's may come
+            # between them on the same stream (the allocator reuses it in stream order)
+            workspace = torch.empty(max(size, 0), dtype=torch.uint8, device=kv.device)
+            ws = workspace.data_ptr()
         else:
             if workspace.get_device() != dev or not workspace.is_contiguous():
                 _bad(f"workspace: a contiguous tensor on cuda:{dev} is needed")
             size, ws = workspace.numel() * workspace.element_size(), workspace.data_ptr()
         rc = lib.dualar_paged_attention(q.data_ptr(), act, max(st[0], h * d), rows, h, c, tab, width, start, lens, n,
                                         window, sinks, d ** -0.5 if scale is None else scale, out.data_ptr(), ldo, ws, size,
-                                        _err(err, dev), stream)
+                                        _err(err, dev), _raw_stream(dev))
     if rc:
         _raise(lib, rc)
     return out

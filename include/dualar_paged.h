@@ -29,7 +29,9 @@
  *     NULL, a bit is OR-ed into *dev_error (DUALAR_PAGED_ERR_*).  The caller
  *     zeroes and reads that word.
  *   - Calls are thread-safe; two calls whose GPU work overlaps need their own
- *     workspaces and outputs.
+ *     workspaces and outputs.  So do two calls that two threads make at once on
+ *     one stream: dualar_paged_attention queues two kernels, and the other
+ *     call's may come between them.
  *
  * Pages follow the decoder's layout.  [P2] of dualar.h ("The slow AR is
  * Qwen3-4B", "Streaming: whose numbers") gives QK-norm and the bf16 rotation

@@ -1,0 +1,59 @@
+"""Paged key/value operators on the GPU as a program calls them: from several
+threads, from other streams, in mixed and padded steps; and the weights' and
+queries' precision by inputs that show it."""
+import threading
+
+import numpy as np
+import pytest
+
+import paged_ref as R
+
+pytestmark = pytest.mark.gpu
+torch = pytest.importorskip("torch")
+PAGE = R.PAGE
+
+
+@pytest.fixture(scope="module", autouse=True)
+def lib_built():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from dual_ar_tts_frame_gb300 import build
+    build()
+
+
+@pytest.fixture
+def gen():
+    g = torch.Generator(device="cuda")
+    g.manual_seed(11)
+    return g
+
+
+def i32(v):
+    return torch.tensor(np.asarray(v, np.int32), device="cuda")
+
+
+@pytest.mark.parametrize("bits,new", [(16, [1, 1]), (4, [1, 1]), (16, [300, 200])])
+def test_two_threads_on_one_stream(gen, bits, new):
+    """Two threads call on the default stream at once, many times, each with its
+    own queries: every output is the one its queries give alone."""
+    from dual_ar_tts_frame_gb300 import paged_attention
+    kv = R.random_layer(150, 8, 128, bits, gen)[:, 0]
+    table, start, lens = R.layout(new, [4000, 5000], 150)
+    qs = [torch.randn((sum(new), 32, 128), generator=gen, device="cuda") for _ in range(2)]
+    want = [paged_attention(q, kv, table, start, lens) for q in qs]
+    torch.cuda.synchronize()
+    got, go = [[], []], threading.Barrier(2)
+
+    def work(i):
+        go.wait()
+        for _ in range(50):
+            got[i].append(paged_attention(qs[i], kv, table, start, lens))
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert len(got[i]) == 50 and all(torch.equal(x, want[i]) for x in got[i])
