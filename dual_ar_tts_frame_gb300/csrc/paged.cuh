@@ -149,12 +149,15 @@ DEVI uint16_t quantize_vector_f64(const float (&x)[EPL], const float (&g)[EPL], 
   bool bad = false;
 #pragma unroll
   for (int j = 0; j < EPL; ++j) y[j] = x[j];
+  // (a warp's vectors may be of different kinds: its lanes add up together,
+  // whether their vector is normed or not)
+  double ss = 0;
+#pragma unroll
+  for (int j = 0; j < EPL; ++j) ss += y[j] * y[j];
+  ss = lanes_sum<L>(ss);
   if (!raw) {
     if (norm) {
-      double ss = 0;
-#pragma unroll
-      for (int j = 0; j < EPL; ++j) ss += y[j] * y[j];
-      const double inv = 1.0 / sqrt(lanes_sum<L>(ss) / (EPL * L) + static_cast<double>(eps));
+      const double inv = 1.0 / sqrt(ss / (EPL * L) + static_cast<double>(eps));
 #pragma unroll
       for (int j = 0; j < EPL; ++j) y[j] = y[j] * inv * static_cast<double>(g[j]);
     }

@@ -57,3 +57,23 @@ def test_two_threads_on_one_stream(gen, bits, new):
     torch.cuda.synchronize()
     for i in range(2):
         assert len(got[i]) == 50 and all(torch.equal(x, want[i]) for x in got[i])
+
+
+@pytest.mark.parametrize("h,hk,d", [(4, 2, 64), (2, 1, 64), (5, 3, 64), (3, 1, 128), (7, 7, 128), (8, 2, 128)])
+@pytest.mark.parametrize("size", [1e-17, 1e17])
+def test_4_bit_keys_that_need_64_bits_beside_values(gen, h, hk, d, size):
+    """Sums of squares outside the fp32 rule's range: every key is computed again
+    in 64 bits, in warps that hold queries and values too."""
+    from dual_ar_tts_frame_gb300 import kv_read, qk_norm_rope, rope_tables
+    rows = 40
+    pool = R.random_layer(2, hk, d, 4, gen)
+    qkv = torch.randn((rows, (h + 2 * hk) * d), generator=gen, device="cuda") * size
+    g = [(1 + 0.2 * torch.randn(d, generator=gen, device="cuda")).to(torch.bfloat16) for _ in range(2)]
+    pos, slot = i32(np.arange(rows) * 3), i32(np.arange(rows) + 50)
+    cos, sin = rope_tables(200, d)
+    qk_norm_rope(qkv, pool[:, 0], pos, slot, *g, cos, sin)
+    x = qkv.double().reshape(rows, -1, d)
+    k = R.norm_rope(x[:, h:h + hk], g[1].double(), cos[pos.long()].double(), sin[pos.long()].double(),
+                    float(np.float32(1e-6)))
+    for got, y in zip(kv_read(pool[:, 0], slot), (k, x[:, h + hk:])):
+        assert torch.equal(got.double(), torch.mul(*R.quantize(y)))
