@@ -93,13 +93,19 @@ def _act(name: str, t: torch.Tensor, dev: int) -> int:
     return a
 
 
+def _ld(stride: int, width: int, rows: int) -> int:
+    """Row stride for the library, which refuses one below the width (rows that
+    overlap, such as expanded ones); a single row's says nothing."""
+    return stride if rows > 1 else width
+
+
 def _out(out: torch.Tensor, like: torch.Tensor, dev: int, rows: int, h: int, d: int) -> int:
     """Row stride of a given output."""
     st = out.stride()
     if (out.dtype is not like.dtype or out.get_device() != dev or out.shape != (rows, h, d) or st[2] != 1 or
             st[1] != d):
         _bad(f"out: {like.dtype} {(rows, h, d)} on cuda:{dev} with contiguous rows is needed")
-    return max(st[0], h * d)
+    return _ld(st[0], h * d, rows)
 
 
 def _err(err, dev: int):
@@ -178,8 +184,8 @@ def qk_norm_rope(qkv: torch.Tensor, kv: torch.Tensor, pos: torch.Tensor, slot: t
     rows, width = qkv.shape if qkv.dim() == 2 else (0, 1)
     h = width // d - 2 * hk
     ld, one = qkv.stride() if qkv.dim() == 2 else (0, 0)
-    if width % d or h < 1 or (one != 1 and rows > 1):
-        _bad(f"qk_norm_rope: qkv {tuple(qkv.shape)} holds no queries beside 2 x {hk} heads of {d}")
+    if width % d or h < 1 or one != 1:
+        _bad(f"qk_norm_rope: qkv {tuple(qkv.shape)} is no matrix of contiguous rows of queries and 2 x {hk} heads of {d}")
     act = _act("qkv", qkv, dev)
     pp, ps = _i32("pos", pos, dev, rows), _i32("slot", slot, dev, rows)
     if q_norm is not None:
@@ -199,7 +205,7 @@ def qk_norm_rope(qkv: torch.Tensor, kv: torch.Tensor, pos: torch.Tensor, slot: t
             out, ldo = torch.empty((rows, h, d), dtype=qkv.dtype, device=kv.device), h * d
         else:
             ldo = _out(out, qkv, dev, rows, h, d)
-        rc = lib.dualar_qk_norm_rope(qkv.data_ptr(), act, max(ld, width), rows, h, c, pp, ps, q_norm, k_norm, eps,
+        rc = lib.dualar_qk_norm_rope(qkv.data_ptr(), act, _ld(ld, width, rows), rows, h, c, pp, ps, q_norm, k_norm, eps,
                                      cos.data_ptr(), sin.data_ptr(), n_pos, out.data_ptr(), ldo, _err(err, dev),
                                      _raw_stream(dev))
     if rc:
@@ -261,7 +267,7 @@ def paged_attention(q: torch.Tensor, kv: torch.Tensor, table: torch.Tensor, row_
             if workspace.get_device() != dev or not workspace.is_contiguous():
                 _bad(f"workspace: a contiguous tensor on cuda:{dev} is needed")
             size, ws = workspace.numel() * workspace.element_size(), workspace.data_ptr()
-        rc = lib.dualar_paged_attention(q.data_ptr(), act, max(st[0], h * d), rows, h, c, tab, width, start, lens, n,
+        rc = lib.dualar_paged_attention(q.data_ptr(), act, _ld(st[0], h * d, rows), rows, h, c, tab, width, start, lens, n,
                                         window, sinks, d ** -0.5 if scale is None else scale, out.data_ptr(), ldo, ws, size,
                                         _err(err, dev), _raw_stream(dev))
     if rc:

@@ -101,3 +101,60 @@ def test_a_workspace_is_given_back(paged, monkeypatch):
     out = attention_call(paged)
     gc.collect()
     assert out.shape == (3, 4, 64) and len(seen) == 1 and seen[0]() is None
+
+
+# ------------------------------------------------------------------- strides --
+
+def rope_call(P, **over):
+    kv = on(P.kv_pool(2, 2, 64, device="cpu"))[:, 0]
+    cos, sin = (on(t) for t in P.rope_tables(8, 64, device="cpu"))
+    a = dict(qkv=on(torch.zeros(3, 8 * 64)), kv=kv, pos=i32(0, 1, 2), slot=i32(0, 1, 2), q_norm=None, k_norm=None, cos=cos,
+             sin=sin)
+    a.update(over)
+    return P.qk_norm_rope(**a)
+
+
+def refused(call, *a, **k):
+    """Refused as an argument, before anything is queued."""
+    with pytest.raises(L.DualARError) as e:
+        call(*a, **k)
+    assert e.value.code == -1, e.value
+
+
+@pytest.mark.parametrize("rows", [3, 2])
+def test_rows_that_overlap_are_refused(paged, rows):
+    """Expanded and overlapping rows hold fewer elements than rows * width: read
+    or written as whole rows they would go past the tensor."""
+    d, start, pos = 64, i32(0, rows), i32(*range(rows))
+    q = on(torch.zeros(rows, 4, d))
+    refused(attention_call, paged, q=q[:1].expand(rows, 4, d), row_start=start)
+    refused(attention_call, paged, q=on(torch.zeros(4 * d + 64 * rows)).as_strided((rows, 4, d), (64, d, 1)), row_start=start)
+    refused(attention_call, paged, q=q, out=q[:1].expand(rows, 4, d), row_start=start)
+    qkv = on(torch.zeros(rows, 8 * d))
+    refused(rope_call, paged, qkv=qkv[:1].expand(rows, 8 * d), pos=pos, slot=pos)
+    refused(rope_call, paged, qkv=qkv, pos=pos, slot=pos, out=q[:1].expand(rows, 4, d))
+
+
+def test_a_row_that_is_not_contiguous_is_refused(paged):
+    """Also where it is the only one."""
+    wide = on(torch.zeros(1, 2 * 8 * 64))
+    refused(rope_call, paged, qkv=wide[:, ::2], pos=i32(0), slot=i32(0))
+    refused(rope_call, paged, qkv=on(torch.zeros(8 * 64, 3)).t())
+    heads = on(torch.zeros(1, 4, 128))
+    refused(attention_call, paged, q=heads[:, :, ::2], row_start=i32(0, 1))
+
+
+@pytest.mark.parametrize("stride", [0, 1, 7, 1001, 10 ** 6])
+def test_the_stride_of_a_single_row_says_nothing(paged, monkeypatch, stride):
+    """A row stride is only used between rows: torch gives a single row any."""
+    got = []
+    lib = Library(L.load(), lambda *a: got.append((a[2], a[15])) or 0)
+    lib.dualar_qk_norm_rope = lambda *a: got.append((a[2], a[15])) or 0
+    monkeypatch.setattr(paged.L, "lib", lambda: lib)
+    base = on(torch.zeros(8 * 64))
+    q = base.as_strided((1, 4, 64), (stride, 64, 1))
+    attention_call(paged, q=q, out=q, row_start=i32(0, 1))
+    rope_call(paged, qkv=base.as_strided((1, 8 * 64), (stride, 1)), pos=i32(0), slot=i32(0), out=q)
+    for ld, ldo in got:
+        assert ld >= 256 and ldo >= 256 and ld % 8 == 0 and ldo % 8 == 0
+    assert len(got) == 2
