@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) kv_plan_kernel(const PlanArgs
   for (int q = q0 + tid; q < q1; q += kPlanThreads) mine += __popc(free_mask(a, q));
   // ---- prefix sums over the requests
   long long rows = 0, pages = 0;
-  bool neg = false, wide = false;
+  bool neg = false, wide = false, bad = false;
   for (int s0 = 0; s0 < a.n_seq; s0 += kPlanThreads) {
     const int s = s0 + tid;
     long long len = 0, add = 0;
@@ -119,6 +119,12 @@ __global__ void __launch_bounds__(kPlanThreads, 1) kv_plan_kernel(const PlanArgs
       add = a.n_new[s];
       neg |= len < 0 || add < 0;
       wide |= (len + add + kPageTokens - 1) / kPageTokens > a.width;
+      // the page that a request's next token goes to is the caller's (the others of
+      // a plan come from the pool): out of range, its slot could be another page's
+      if (add > 0 && len > 0 && len % kPageTokens && len / kPageTokens < a.width) {
+        const int page = a.table[static_cast<int64_t>(s) * a.width + len / kPageTokens];
+        bad |= page < 0 || page >= a.n_pages;
+      }
     }
     long long r = add, p = (len + add + kPageTokens - 1) / kPageTokens - (len + kPageTokens - 1) / kPageTokens, tr, tp;
     block_scan2(r, p, tot, &tr, &tp);
@@ -134,6 +140,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) kv_plan_kernel(const PlanArgs
   if (lane == 0) warp_tot[warp] = mine;
   neg = __syncthreads_or(neg);
   wide = __syncthreads_or(wide);
+  bad = __syncthreads_or(bad);
   if (warp == 0) {
     const int v = __reduce_add_sync(0xffffffffu, warp_tot[lane]);
     if (lane == 0) my_free = v;
@@ -149,6 +156,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) kv_plan_kernel(const PlanArgs
   if (pages > free_pages) code = 1;
   if (wide) code = 2;
   if (rows > a.max_rows) code = 4;
+  if (bad) code = 5;
   if (neg) {
     code = 3;
     rows = pages = 0;

@@ -96,8 +96,9 @@ int64_t dualar_kv_page_bytes(int32_t n_kv_head, int32_t head_dim, int32_t bits);
  * no row (row_start all 0, every slot -1, new_len = kv_len): status[0] is then 3
  * (a negative length; rows and pages are 0) or else the highest that holds of 1
  * (more pages needed than are free), 2 (a request needs more than table_width
- * pages) and 4 (more than max_rows rows), followed by the rows and pages that
- * the step would need (at most 2^31 - 1).
+ * pages), 4 (more than max_rows rows) and 5 (the table's entry of a partly filled
+ * page that gets tokens is outside [0, n_pages)), followed by the rows and pages
+ * that the step would need (at most 2^31 - 1).
  * A page is released by lowering its page_refs (a shared prefix counts its
  * holders).  n_seq <= 8192, max_rows <= 2^24, table_width <= 2^20.  Outputs may
  * not overlap inputs, but new_len may be kv_len. */

@@ -77,3 +77,28 @@ def test_4_bit_keys_that_need_64_bits_beside_values(gen, h, hk, d, size):
                     float(np.float32(1e-6)))
     for got, y in zip(kv_read(pool[:, 0], slot), (k, x[:, h + hk:])):
         assert torch.equal(got.double(), torch.mul(*R.quantize(y)))
+
+
+@pytest.mark.parametrize("n", [2, 1500])
+@pytest.mark.parametrize("page", [-1, 9000, 1 << 25, 1 << 30, -(1 << 31)])
+def test_a_plan_into_a_page_out_of_range_is_refused(n, page):
+    """The page of a request's last tokens is the caller's table entry: where it is
+    out of range (times 64 it may even wrap to another page's slots) nothing is
+    planned.  An entry that gets no token is not looked at."""
+    from dual_ar_tts_frame_gb300 import kv_plan
+    refs, table = i32(np.zeros(9000)), i32(np.arange(3 * n).reshape(n, 3))
+    refs[:3 * n] = 1
+    lens, new = np.full(n, 70), np.full(n, 3)
+    bad = n - 1
+    table[bad, 1] = page
+    keep = refs.clone(), table.clone()
+    p = kv_plan(i32(lens), i32(new), refs, table, 3 * n + 5)
+    assert p.status.tolist() == [5, 3 * n, 0] and (p.slot == -1).all() and (p.pos == 0).all()
+    assert (p.row_start == 0).all() and p.new_len.tolist() == lens.tolist()
+    assert torch.equal(refs, keep[0]) and torch.equal(table, keep[1])
+    new[bad] = 0                                 # no token for it
+    assert kv_plan(i32(lens), i32(new), refs, table, 3 * n + 5).status.tolist() == [0, 3 * n - 3, 0]
+    new[bad], lens[bad] = 3, 64                  # its next token goes to a new page
+    table[bad, 1:] = page
+    p = kv_plan(i32(lens), i32(new), refs, table, 3 * n + 5)
+    assert p.status.tolist() == [0, 3 * n, 1] and p.slot[3 * n - 3:3 * n].tolist() == [3 * n * 64 + i for i in range(3)]
