@@ -699,8 +699,10 @@ __global__ void __launch_bounds__(Pro<HD, BITS, F32>::THREADS, 1)
       if constexpr (H > 1) {
         // the other shares' (also: all have read their scores, which the weights overwrite)
         row_max[b & 1][share][row] = mx;
+        tc_fence_before();
         mbar_arrive(&rowx);
         if (!mbar_wait(&rowx, b & 1, a.err, kPromptWaitNs)) break;
+        tc_fence_after();
 #pragma unroll
         for (int h = 0; h < H; ++h) mx = fmaxf(mx, row_max[b & 1][h][row]);
       }
