@@ -70,7 +70,11 @@ struct AttnArgs {
   int64_t ldo;
   float* ws;
   uint32_t* err;
+  int32_t no_waiting;    // tests: the waits inside the kernel for many rows run out at once
 };
+// The workspace begins with a header per CTA: of its unfinished last unit, for the
+// join, and (kHeadLost) whether a wait of the CTA ran out.  Then the pieces.
+constexpr int kHeadInts = 8, kHeadLost = 6;
 // Few rows per request (paged_decode.cu), then the join of units that fell on
 // several CTAs.
 cudaError_t launch_attn_decode(const AttnArgs& a, bool bf16, int n_sm, cudaStream_t st);

@@ -90,9 +90,6 @@ struct DecChunk {
 };
 constexpr int kPageOk = 1, kUnitEnd = 2, kBegins = 4;
 
-// Header of a CTA's unfinished last unit, for the join (ints).
-constexpr int kDecHeadInts = 8;
-
 DEVI void ldsm4(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -270,8 +267,8 @@ __global__ void __launch_bounds__(Dec<HD, BITS, F32>::WARPS * 32, Dec<HD, BITS, 
   if (tid < W * 2) seg[tid >> 1][tid & 1].used = 0;
   find_share<TILE, CT, W * 32>(a, group, W, sc);
   const AttnShare sh = sc.share;
-  int* heads = reinterpret_cast<int*>(a.ws) + blockIdx.x * kDecHeadInts;
-  float* parts = a.ws + gridDim.x * kDecHeadInts;
+  int* heads = reinterpret_cast<int*>(a.ws) + blockIdx.x * kHeadInts;
+  float* parts = a.ws + gridDim.x * kHeadInts;
   if (tid == 0) heads[0] = 0;
   if (sh.w0 >= sh.w1) return;   // the whole CTA
   unsigned char* ring = smem + warp * D::RING;
@@ -853,6 +850,16 @@ __global__ void __launch_bounds__(Dec<HD, BITS, F32>::WARPS * 32, Dec<HD, BITS, 
   }
 }
 
+// NaN in all rows of the call: a wait of the attention kernel ran out, and which rows
+// are right is not known.
+template <int HD, bool F32>
+__device__ __noinline__ void rows_are_lost(const AttnArgs& a) {
+  const int end = min(a.rows, a.row_start[a.n_seq]), width = a.n_head * HD;
+  const float nan[2] = {NAN, NAN};
+  for (int row = max(0, a.row_start[0]) + blockIdx.y * gridDim.x + blockIdx.x; row < end; row += gridDim.x * gridDim.y)
+    for (int i = threadIdx.x * 2; i < width; i += 512) store_act<!F32, 2>(a.out, static_cast<int64_t>(row) * a.ldo + i, nan);
+}
+
 // Joins the units that several CTAs worked on, in CTA order: CTA c's header
 // names the unit that began in it, whose pieces are (c, 1), (c + 1, 0), ..  A warp
 // per row, 8 rows a CTA.  The weights e^(m_i - m) and sums are fp32, added in piece
@@ -863,11 +870,19 @@ template <int HD, bool F32, int TILE>
 __global__ void __launch_bounds__(256) attn_join_kernel(const AttnArgs a, int n_cta) {
   constexpr int PART = TILE * (HD + 2), E = HD / 32;
   pdl_wait();
-  const int4* h4 = reinterpret_cast<const int4*>(a.ws) + blockIdx.x * (kDecHeadInts / 4);
+  if constexpr (TILE != kDecTile) {
+    bool lost = false;
+    for (int c = threadIdx.x; c < n_cta; c += 256) lost |= reinterpret_cast<const int*>(a.ws)[c * kHeadInts + kHeadLost] != 0;
+    if (__syncthreads_or(lost)) {
+      rows_are_lost<HD, F32>(a);
+      return;
+    }
+  }
+  const int4* h4 = reinterpret_cast<const int4*>(a.ws) + blockIdx.x * (kHeadInts / 4);
   const int4 h = h4[0], h2 = h4[1];
   const int r = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (!h.x || r >= h2.x) return;
-  const float* parts = a.ws + n_cta * kDecHeadInts;
+  const float* parts = a.ws + n_cta * kHeadInts;
   const int group = a.n_head / a.kv.n_kv_head, n = h.y + 1;
   float acc[E], m = -FLT_MAX, l = 0.f;
 #pragma unroll
@@ -910,7 +925,7 @@ static cudaError_t launch_one(const AttnArgs& a, int n_sm, cudaStream_t st) {
 
 int64_t decode_workspace_floats(int bits, int head_dim) {
   const int64_t grid = kAttnSms * (bits == 4 ? 2 : 1), part = kDecTile * (head_dim + 2);
-  return grid * (kDecHeadInts + 2 * part);
+  return grid * (kHeadInts + 2 * part);
 }
 
 cudaError_t launch_attn_decode(const AttnArgs& a, bool bf16, int n_sm, cudaStream_t st) {

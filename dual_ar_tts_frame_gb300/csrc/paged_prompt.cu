@@ -52,7 +52,9 @@
 
 namespace dualar {
 
-constexpr uint64_t kPromptWaitNs = 2000000000ull;   // limit of every wait inside the kernel
+// Limit of every wait inside the kernel.  A constant: read from the arguments it costs
+// fp32 rows over 4 bits 3% (two prompts: 488 us instead of 474).
+constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr float kLazyMax = 8.f;                     // a row's maximum may lag by this (log2)
 
 template <int HD, int BITS, bool F32>
@@ -85,7 +87,6 @@ struct Pro {
   static constexpr int PART = TILE * (HD + 2);       // floats of a partial result
 };
 
-constexpr int kJoinHeadInts = 8;
 // Blocks whose scales are kept.  A slot ring of NSLOT <= 8 lets the loaders run at
 // most NSLOT / 2 + 1 blocks ahead of the rows, so a block's entry is free again
 // when they come back to it.
@@ -206,6 +207,7 @@ __global__ void __launch_bounds__(Pro<HD, BITS, F32>::THREADS, 1)
   __shared__ ShareScratch<D::THREADS> sc;
   __shared__ uint64_t full[NSLOT], empty[NSLOT], qfull, qempty, sfull[NT * RB], pready[NT], odone[NT], drained, bready[kMeta], rowx, suml;
   __shared__ uint32_t tmem_slot;
+  __shared__ int gave_up;                              // a wait ran out
   __shared__ float row_max[2][H][H > 1 ? 128 : 1], row_sum[H][H > 1 ? 128 : 1];   // the shares' maxima (two blocks) and sums
   // what the rows need of a block beside its products; block b's is at b % kMeta
   __shared__ int page_ok[kMeta];                       // per 64 tokens: the page is in range
@@ -218,6 +220,7 @@ __global__ void __launch_bounds__(Pro<HD, BITS, F32>::THREADS, 1)
   constexpr int MMA_WARP = D::ROWS / 32, LOAD0 = D::ROWS + 32;
 
   if (tid == 0) {
+    gave_up = a.no_waiting;
     for (int s = 0; s < NSLOT; ++s) {
       mbar_init(&full[s], LT);
       mbar_init(&empty[s], 1);
@@ -239,10 +242,24 @@ __global__ void __launch_bounds__(Pro<HD, BITS, F32>::THREADS, 1)
   pdl_launch();
   find_share<TILE, BT, D::THREADS>(a, group, 1, sc);
   const AttnShare sh = sc.share;
-  int* heads = reinterpret_cast<int*>(a.ws) + blockIdx.x * kJoinHeadInts;
-  float* parts = a.ws + gridDim.x * kJoinHeadInts;
-  if (tid == 0) heads[0] = 0;
+  int* heads = reinterpret_cast<int*>(a.ws) + blockIdx.x * kHeadInts;
+  float* parts = a.ws + gridDim.x * kHeadInts;
+  if (tid == 0) heads[0] = heads[kHeadLost] = 0;
   if (sh.w0 >= sh.w1) return;   // the whole CTA
+  // Every wait of the roles has a limit; behind one that ran out no other waits any
+  // more.  What the CTA leaves behind is then not the call's result: the join, told by
+  // its header, makes all rows NaN.
+  auto reached = [&](uint64_t* bar, int phase) {
+    if (mbar_try_wait(bar, phase & 1)) return true;
+    const uint64_t t0 = global_timer_ns();
+    while (!mbar_try_wait(bar, phase & 1))
+      if (*const_cast<volatile int*>(&gave_up) || global_timer_ns() - t0 > kWaitNs) {
+        raise_error(a.err, DEV_ERR_MBAR_TIMEOUT);
+        gave_up = 1;
+        return false;
+      }
+    return true;
+  };
   if (warp == MMA_WARP) {
     tmem_alloc(&tmem_slot, D::ALLOC);
     tmem_relinquish();
@@ -340,7 +357,7 @@ __global__ void __launch_bounds__(Pro<HD, BITS, F32>::THREADS, 1)
     for (int b = 0; b < n_blocks; ++b) {
       if (!F32 && fresh) {
         fresh = false;
-        if (unit_n > 0 && !mbar_wait(&qempty, (unit_n - 1) & 1, a.err, kPromptWaitNs)) break;
+        if (unit_n > 0 && !reached(&qempty, unit_n - 1)) break;
         ++unit_n;
         const RowMap rows(wk.u.r0, group);
         if (use_tma & 2) {
@@ -402,7 +419,7 @@ __global__ void __launch_bounds__(Pro<HD, BITS, F32>::THREADS, 1)
 #pragma unroll 1
       for (int kv = 0; kv < 2; ++kv) {
         const int n = 2 * b + kv, slot = n % NSLOT;
-        if (n >= NSLOT && !mbar_wait(&empty[slot], (n / NSLOT - 1) & 1, a.err, kPromptWaitNs)) {
+        if (n >= NSLOT && !reached(&empty[slot], n / NSLOT - 1)) {
           dead = true;
           break;
         }
@@ -463,11 +480,12 @@ __global__ void __launch_bounds__(Pro<HD, BITS, F32>::THREADS, 1)
       mbar_arrive(&bready[b % kMeta]);
       fresh = next_fresh;
     }
-    // every copy issued here has landed before the CTA may exit (bounded)
+    // every copy issued here has landed before the CTA may exit (where other loaders
+    // gave up, a barrier stays open: one limit is enough for all copies)
     if (t == 0) {
-      if (!F32 && unit_n > 0) mbar_wait(&qfull, (unit_n - 1) & 1, a.err, kPromptWaitNs);
-      for (int n = issued > NSLOT ? issued - NSLOT : 0; n < issued; ++n)
-        mbar_wait(&full[n % NSLOT], (n / NSLOT) & 1, a.err, kPromptWaitNs);
+      bool landed = F32 || unit_n == 0 || mbar_wait(&qfull, (unit_n - 1) & 1, a.err, kWaitNs);
+      for (int n = issued > NSLOT ? issued - NSLOT : 0; n < issued && landed; ++n)
+        landed = mbar_wait(&full[n % NSLOT], (n / NSLOT) & 1, a.err, kWaitNs);
     }
   } else if (warp == MMA_WARP) {
     if (lane == 0) {
@@ -503,7 +521,7 @@ __global__ void __launch_bounds__(Pro<HD, BITS, F32>::THREADS, 1)
       };
       auto wait = [&](uint64_t* bar, int phase) {
         if (dead) return;
-        if (!mbar_wait(bar, phase & 1, a.err, kPromptWaitNs)) dead = true;
+        if (!reached(bar, phase)) dead = true;
         tc_fence_after();
       };
       bool fresh = true;                      // the block begins its unit
@@ -557,10 +575,23 @@ __global__ void __launch_bounds__(Pro<HD, BITS, F32>::THREADS, 1)
       }
       // every MMA issued has completed before the CTA gives its memory back
       tc_commit(&drained);
-      mbar_wait(&drained, 0, a.err, kPromptWaitNs);
+      mbar_wait(&drained, 0, a.err, kWaitNs);
     }
   } else {
     // ---- rows: thread = row of its tile (fp32: four threads, a share each)
+    // (all lanes of a warp go on or stop together: its tensor-memory instructions take
+    // them all)
+    auto ready = [&](uint64_t* bar, int phase) {
+      if (__all_sync(0xffffffffu, mbar_try_wait(bar, phase & 1))) return true;
+      const uint64_t t0 = global_timer_ns();
+      while (!__all_sync(0xffffffffu, mbar_try_wait(bar, phase & 1)))
+        if (__any_sync(0xffffffffu, *const_cast<volatile int*>(&gave_up) || global_timer_ns() - t0 > kWaitNs)) {
+          raise_error(a.err, DEV_ERR_MBAR_TIMEOUT);
+          gave_up = 1;
+          return false;
+        }
+      return true;
+    };
     const int tile = H > 1 ? 0 : warp >> 2, share = H > 1 ? warp >> 2 : 0, row = tid & 127;
     constexpr int HDH = HD / H;              // dims of a thread
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
@@ -579,7 +610,7 @@ __global__ void __launch_bounds__(Pro<HD, BITS, F32>::THREADS, 1)
         fresh = false;
         if constexpr (F32) {
           // the unit's queries in parts: four loads in flight per thread
-          if (!first && !mbar_wait(&qempty, (units - 1) & 1, a.err, kPromptWaitNs)) break;
+          if (!first && !ready(&qempty, units - 1)) break;
           constexpr int QB = TILE * PR / D::ROWS < 4 ? TILE * PR / D::ROWS : 4;
           static_assert(TILE * PR % (D::ROWS * QB) == 0, "whole rounds");
           const RowMap rows(wk.u.r0, group);
@@ -643,8 +674,8 @@ __global__ void __launch_bounds__(Pro<HD, BITS, F32>::THREADS, 1)
       }
       const int pos = wk.pos, meta = b % kMeta;
       const uint32_t ts = ts0 + (b % RB) * D::SCOLS;
-      if (!mbar_wait(&sfull[tile * RB + b % RB], (b / RB) & 1, a.err, kPromptWaitNs)) break;
-      if (!mbar_wait(&bready[meta], (b / kMeta) & 1, a.err, kPromptWaitNs)) break;
+      if (!ready(&sfull[tile * RB + b % RB], b / RB)) break;
+      if (!ready(&bready[meta], b / kMeta)) break;
       tc_fence_after();
       const int okm = page_ok[meta];
       bool see_all = okm == (1 << (BT / 64)) - 1 && pos + BT <= pmin + 1 && pos + BT <= wk.u.hi;
@@ -701,7 +732,7 @@ __global__ void __launch_bounds__(Pro<HD, BITS, F32>::THREADS, 1)
         row_max[b & 1][share][row] = mx;
         tc_fence_before();
         mbar_arrive(&rowx);
-        if (!mbar_wait(&rowx, b & 1, a.err, kPromptWaitNs)) break;
+        if (!ready(&rowx, b)) break;
         tc_fence_after();
 #pragma unroll
         for (int h = 0; h < H; ++h) mx = fmaxf(mx, row_max[b & 1][h][row]);
@@ -767,7 +798,7 @@ __global__ void __launch_bounds__(Pro<HD, BITS, F32>::THREADS, 1)
       tmem_wait_st();
       // fp32: block b's output, added to the running one
       auto take_output = [&](int b, float scale) {
-        if (!mbar_wait(&odone[tile], b & 1, a.err, kPromptWaitNs)) return false;
+        if (!ready(&odone[tile], b)) return false;
         tc_fence_after();
 #pragma unroll
         for (int ch = 0; ch < HDH / 16; ++ch) {
@@ -797,14 +828,14 @@ __global__ void __launch_bounds__(Pro<HD, BITS, F32>::THREADS, 1)
           tc_fence_before();
         }
       } else if (last) {
-        if (!mbar_wait(&odone[tile], b & 1, a.err, kPromptWaitNs)) break;
+        if (!ready(&odone[tile], b)) break;
         tc_fence_after();
       }
       if (last) {
         if constexpr (H > 1) {
           row_sum[share][row] = l;
           mbar_arrive(&suml);
-          if (!mbar_wait(&suml, units & 1, a.err, kPromptWaitNs)) break;
+          if (!ready(&suml, units)) break;
           l = row_sum[0][row];
 #pragma unroll
           for (int h = 1; h < H; ++h) l += row_sum[h][row];
@@ -911,6 +942,7 @@ __global__ void __launch_bounds__(Pro<HD, BITS, F32>::THREADS, 1)
     tc_fence_after();
     tmem_dealloc(tm, D::ALLOC);
   }
+  if (tid == 0) heads[kHeadLost] = gave_up;
 }
 
 using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
@@ -969,7 +1001,7 @@ static cudaError_t launch_one(const AttnArgs& a, int n_sm, cudaStream_t st) {
 }
 
 int64_t prompt_workspace_floats(bool f32, int head_dim) {
-  return static_cast<int64_t>(kAttnSms) * (kJoinHeadInts + 2 * (f32 ? 128 : 256) * (head_dim + 2));
+  return static_cast<int64_t>(kAttnSms) * (kHeadInts + 2 * (f32 ? 128 : 256) * (head_dim + 2));
 }
 
 cudaError_t launch_attn_prompt(const AttnArgs& a, bool bf16, int n_sm, cudaStream_t st) {

@@ -286,10 +286,12 @@ def paged_attention_workspace(q: torch.Tensor, kv: torch.Tensor, n_seq: int) -> 
 
 def check_errors(err: torch.Tensor) -> None:
     """Synchronises with the work that reports into err, raises DualARError
-    (DUALAR_ERR_DEVICE) if a bounds check failed on the device, and clears it."""
+    (DUALAR_ERR_DEVICE) if a bounds check failed on the device or a wait there
+    ran out, and clears it."""
     word = int(err.item())
     if word:
         err.zero_()
-        what = [s for b, s in ((4, "a row, slot, position or length out of range"), (8, "a page out of range"))
+        what = [s for b, s in ((1, "a wait inside a kernel that ran out"),
+                               (4, "a row, slot, position or length out of range"), (8, "a page out of range"))
                 if word & b]
         raise L.DualARError(-7, " and ".join(what) or f"error word 0x{word:x}")

@@ -339,7 +339,8 @@ int dualar_read_state(dualar_handle* h, int32_t slot, float* hidden, float* logi
 /* Next position of a slot (prompt length + frames decoded); -1 if empty. */
 int32_t dualar_slot_length(const dualar_handle* h, int32_t slot);
 
-/* Time limit of every device-side wait, in nanoseconds (default 2 s). */
+/* Time limit of every device-side wait, in nanoseconds (default 2 s; those inside
+ * the attention with a window keep 2 s). */
 int dualar_set_wait_limit(dualar_handle* h, uint64_t nanoseconds);
 
 /* Number of kernel launches queued by the last decode call. */

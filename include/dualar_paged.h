@@ -56,6 +56,7 @@ enum { DUALAR_F32 = 0, DUALAR_BF16 = 1 };
 
 /* Bits of *dev_error. */
 enum {
+  DUALAR_PAGED_ERR_WAIT = 1 << 0,  /* a wait inside a kernel ran out (see dualar_paged_attention) */
   DUALAR_PAGED_ERR_INDEX = 1 << 2, /* a row, slot, position or length out of range */
   DUALAR_PAGED_ERR_PAGE = 1 << 3   /* a page-table entry out of range */
 };
@@ -152,7 +153,10 @@ int64_t dualar_paged_attention_workspace(int32_t act, int32_t rows, int32_t n_he
  * value that one row of a request sees may reach its other rows of the call.
  * Sums and softmax statistics are fp32.  fp32 activations: queries and weights
  * keep 16 significant bits at least; bf16: eight.
- * The result depends on the arguments and the device alone, not on timing.
+ * The result depends on the arguments and the device alone, not on timing; but
+ * for waits inside the kernels, which end after 2 s (a device taken from the call
+ * meanwhile): every row of the call is then NaN and *dev_error has
+ * DUALAR_PAGED_ERR_WAIT.
  * n_head / n_kv_head <= 32, rows <= 2^24, table_width <= 2^20, n_seq <= 8192;
  * workspace: dualar_paged_attention_workspace bytes, 16-byte aligned, any
  * contents. */

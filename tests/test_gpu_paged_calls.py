@@ -1,6 +1,9 @@
 """Paged key/value operators on the GPU as a program calls them: from several
 threads, from other streams, in mixed and padded steps; and the weights' and
 queries' precision by inputs that show it."""
+import ctypes
+import os
+import subprocess
 import threading
 
 import numpy as np
@@ -102,3 +105,76 @@ def test_a_plan_into_a_page_out_of_range_is_refused(n, page):
     table[bad, 1:] = page
     p = kv_plan(i32(lens), i32(new), refs, table, 3 * n + 5)
     assert p.status.tolist() == [0, 3 * n, 1] and p.slot[3 * n - 3:3 * n].tolist() == [3 * n * 64 + i for i in range(3)]
+
+
+SHIM = r"""
+#include "paged.h"
+// The prompt kernel and its join; no_waiting: its waits run out at once.
+extern "C" int prompt_call(const void* q, int rows, int n_head, void* kv, long long stride, int n_pages, int hk,
+                                 int hd, int bits, const int* table, int width, const int* row_start, const int* kv_len,
+                                 int n_seq, void* out, void* ws, unsigned* err, int bf16, int no_waiting, void* stream) {
+  dualar::AttnArgs a{};
+  a.q = q;
+  a.ldq = a.ldo = static_cast<long long>(n_head) * hd;
+  a.rows = rows;
+  a.n_head = n_head;
+  a.kv = dualar::KvView{static_cast<unsigned char*>(kv), stride, n_pages, hk, hd, bits};
+  a.table = table;
+  a.width = width;
+  a.row_start = row_start;
+  a.kv_len = kv_len;
+  a.n_seq = n_seq;
+  a.scale = 0.1f;
+  a.out = out;
+  a.ws = static_cast<float*>(ws);
+  a.err = err;
+  a.no_waiting = no_waiting;
+  return dualar::launch_attn_prompt(a, bf16 != 0, dualar::kAttnSms, static_cast<cudaStream_t>(stream));
+}
+"""
+
+
+@pytest.fixture(scope="module")
+def shim(tmp_path_factory):
+    from dual_ar_tts_frame_gb300 import _lib as L
+    L.load()
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    csrc, include = os.path.join(root, "dual_ar_tts_frame_gb300", "csrc"), os.path.join(root, "include")
+    out = tmp_path_factory.mktemp("shim")
+    (out / "shim.cpp").write_text(SHIM)
+    so = str(out / "shim.so")
+    subprocess.check_call(["g++", "-std=c++17", "-shared", "-fPIC", "-I", csrc, "-I", include, "-I", "/usr/local/cuda/include",
+                           str(out / "shim.cpp"), "-o", so, L.LIB_PATH, f"-Wl,-rpath,{os.path.dirname(L.LIB_PATH)}"])
+    f = ctypes.CDLL(so).prompt_call
+    f.argtypes = [ctypes.c_void_p, ctypes.c_int, ctypes.c_int, ctypes.c_void_p, ctypes.c_longlong] + [ctypes.c_int] * 4 + [
+        ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int] + [ctypes.c_void_p] * 3 + [
+        ctypes.c_int, ctypes.c_int, ctypes.c_void_p]
+    return f
+
+
+@pytest.mark.parametrize("bits", [16, 4])
+@pytest.mark.parametrize("act", [torch.float32, torch.bfloat16])
+def test_a_wait_that_runs_out_leaves_no_wrong_rows(gen, shim, bits, act):
+    """Where the kernel's waits run out (here: at once) all rows are NaN
+    (not those of the units that ended in time only), rows behind the last request
+    stay as they were, and the error word says so.  With the usual limit the same
+    call is right behind it."""
+    from dual_ar_tts_frame_gb300 import paged_attention
+    h, hk, d, new, ctx = 8, 2, 128, [300, 500], [900, 700]
+    kv = R.random_layer(30, hk, d, bits, gen)[:, 0]
+    table, start, lens = R.layout(new, ctx, 30)
+    q = torch.randn((sum(new) + 4, h, d), generator=gen, device="cuda").to(act)
+    want = paged_attention(q, kv, table, start, lens, scale=0.1)
+    ws = torch.zeros(50 << 20, dtype=torch.uint8, device="cuda")
+    for no_waiting in (0, 1, 0):
+        out, err = torch.full_like(q, 3.0), i32([0])
+        rc = shim(q.data_ptr(), sum(new) + 4, h, kv.data_ptr(), kv.stride(0) * kv.element_size(), 30, hk, d, bits,
+                  table.data_ptr(), table.shape[1], start.data_ptr(), lens.data_ptr(), 2, out.data_ptr(), ws.data_ptr(),
+                  err.data_ptr(), act == torch.bfloat16, no_waiting, torch.cuda.current_stream().cuda_stream)
+        assert rc == 0
+        torch.cuda.synchronize()
+        assert (out[sum(new):] == 3).all()
+        if no_waiting:
+            assert int(err.item()) == 1 and torch.isnan(out[:sum(new)]).all()
+        else:
+            assert int(err.item()) == 0 and torch.equal(out[:sum(new)], want[:sum(new)])

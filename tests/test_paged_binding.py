@@ -3,6 +3,8 @@ tensors in host memory that say they are on device 0, with the library's entry
 point replaced where a call would go on to the device."""
 import ctypes
 import gc
+import os
+import re
 import threading
 import weakref
 
@@ -12,6 +14,8 @@ from dual_ar_tts_frame_gb300 import _lib as L
 from dual_ar_tts_frame_gb300.build import build
 
 torch = pytest.importorskip("torch")
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 class OnDevice(torch.Tensor):
@@ -158,3 +162,16 @@ def test_the_stride_of_a_single_row_says_nothing(paged, monkeypatch, stride):
     for ld, ldo in got:
         assert ld >= 256 and ldo >= 256 and ld % 8 == 0 and ldo % 8 == 0
     assert len(got) == 2
+
+
+# -------------------------------------------------------------- error reports --
+
+@pytest.mark.parametrize("word,says", [(1, "wait"), (4, "slot"), (8, "page"), (5, "wait.* and .*slot")])
+def test_every_bit_of_the_error_word_is_named(paged, word, says):
+    header = open(os.path.join(ROOT, "include", "dualar_paged.h")).read()
+    bits = dict(re.findall(r"(DUALAR_PAGED_ERR_\w+) = 1 << (\d)", header))
+    assert sorted(bits.values()) == ["0", "2", "3"]
+    err = torch.tensor([word], dtype=torch.int32)
+    with pytest.raises(L.DualARError, match=says) as e:
+        paged.check_errors(err)
+    assert e.value.code == -7 and err.item() == 0

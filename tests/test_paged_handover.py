@@ -28,7 +28,7 @@ def test_arrivals_follow_a_fence(barrier):
 @pytest.mark.parametrize("barrier", ["rowx", "odone", "sfull"])
 def test_waits_are_followed_by_a_fence(barrier):
     code = lines()
-    at = [i for i, x in enumerate(code) if re.search(r"(mbar_wait|reached)\(&%s\b" % barrier, x)]
+    at = [i for i, x in enumerate(code) if re.search(r"(mbar_wait|reached|ready)\(&%s\b" % barrier, x)]
     assert at
     for i in at:
         # (sfull's wait and the block's next are fenced together)
