@@ -70,6 +70,14 @@ class dualar_sampling(ctypes.Structure):
                 ("ras_temperature", c_f32), ("ras_top_p", c_f32), ("allow_eos", c_i32)]
 
 
+def check_int32(**values: int) -> None:
+    """Refuses integers that the library would get only the low bits of (ctypes
+    drops the others)."""
+    for name, v in values.items():
+        if not -2 ** 31 <= v < 2 ** 31:
+            raise DualARError(-1, f"{name} {v} is no 32-bit integer")
+
+
 class dualar_kv(ctypes.Structure):
     _fields_ = [("data", c_vp), ("page_stride", c_i64)] + [(n, c_i32) for n in (
         "n_pages", "n_kv_head", "head_dim", "bits")]

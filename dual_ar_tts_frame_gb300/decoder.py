@@ -258,6 +258,7 @@ class DualARDecoder:
     def set_attn_window(self, window: int, sinks: int = 0) -> None:
         """Slow attention over the last `window` positions and the first `sinks`
         (0: every position)."""
+        L.check_int32(window=window, sinks=sinks)
         self._check(self.lib.dualar_set_attn_window(self.h, window, sinks))
 
     def debug_barrier_extra(self, extra: int) -> None:

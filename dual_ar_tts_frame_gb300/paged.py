@@ -123,6 +123,7 @@ def _on(dev: int):
 
 def kv_page_bytes(n_kv_head: int, head_dim: int, bits: int = 16) -> int:
     """Bytes of one layer of one page."""
+    L.check_int32(n_kv_head=n_kv_head, head_dim=head_dim, bits=bits)
     n = L.lib().dualar_kv_page_bytes(n_kv_head, head_dim, bits)
     if n < 0:
         _bad(f"kv: {n_kv_head} heads of {head_dim} in {bits} bits (head_dim 64 or 128, bits 16 or 4)")
@@ -155,8 +156,9 @@ def kv_plan(kv_len: torch.Tensor, n_new: torch.Tensor, page_refs: torch.Tensor, 
     place in page_refs [n_pages] and table [n_seq, width]) and lays out the
     step's rows."""
     dev = kv_len.get_device()
-    if dev < 0 or kv_len.dim() != 1 or table.dim() != 2 or page_refs.dim() != 1 or max_rows < 0:
-        _bad("kv_plan: kv_len is [n_seq] on a CUDA device, table [n_seq, width], page_refs [n_pages], max_rows >= 0")
+    if dev < 0 or kv_len.dim() != 1 or table.dim() != 2 or page_refs.dim() != 1 or not (
+            0 <= max_rows <= 2 ** 24):
+        _bad("kv_plan: kv_len is [n_seq] on a CUDA device, table [n_seq, width], page_refs [n_pages], max_rows in [0, 2^24]")
     n, (nt, width) = kv_len.shape[0], table.shape
     if nt != n:
         _bad(f"kv_plan: a table of {nt} rows for {n} requests")
@@ -217,6 +219,7 @@ def kv_read(kv: torch.Tensor, slot: torch.Tensor, err: torch.Tensor | None = Non
     """dualar_kv_read: keys and values of slots as float32 [n, n_kv_head, head_dim]."""
     c, dev, n, lib = _kv(kv), kv.get_device(), slot.numel(), L.lib()
     ps = _i32("slot", slot, dev)
+    L.check_int32(slots=n)
     shape = (n, c.n_kv_head, c.head_dim)
     with _on(dev):
         k = torch.empty(shape, dtype=_F32, device=kv.device)
@@ -245,6 +248,7 @@ def paged_attention(q: torch.Tensor, kv: torch.Tensor, table: torch.Tensor, row_
     if dq != d or st[2] != 1 or st[1] != d:
         _bad(f"paged_attention: q {tuple(q.shape)}: [rows, n_head, {d}] with contiguous rows is needed")
     act = _act("q", q, dev)
+    L.check_int32(window=window, sinks=sinks)
     if kv_len.dim() != 1 or table.dim() != 2:
         _bad("paged_attention: kv_len is [n_seq], table [n_seq, width]")
     n, (nt, width) = kv_len.shape[0], table.shape

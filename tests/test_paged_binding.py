@@ -175,3 +175,17 @@ def test_every_bit_of_the_error_word_is_named(paged, word, says):
     with pytest.raises(L.DualARError, match=says) as e:
         paged.check_errors(err)
     assert e.value.code == -7 and err.item() == 0
+
+
+# ------------------------------------------------------------------- integers --
+
+@pytest.mark.parametrize("big", [2 ** 31, 2 ** 32, 2 ** 32 + 5, 2 ** 63, -2 ** 32 + 5, -1])
+def test_integers_that_no_int32_holds_are_refused(paged, big):
+    """ctypes keeps an integer's low bits: a window of 2^32 + 5 would be one of 5."""
+    refused(attention_call, paged, window=big)
+    refused(attention_call, paged, window=7, sinks=big)
+    refused(paged.kv_plan, i32(3), i32(1), i32(0), i32(0)[None], big)
+    for shape in ((big, 64, 16), (8, big, 16), (8, 64, big)):
+        refused(paged.kv_page_bytes, *shape)
+        refused(paged.kv_pool, 1, *shape, device="cpu")
+    refused(paged.kv_plan, i32(3), i32(1), i32(0), i32(0)[None], 2 ** 24 + 1)

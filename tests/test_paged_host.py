@@ -203,3 +203,24 @@ def test_plain_attention_by_hand():
 
 def test_window_needs_a_handle(lib):
     assert lib.dualar_set_attn_window(None, 4, 0) == -1
+
+
+@pytest.mark.parametrize("window,sinks", [(2 ** 31, 0), (2 ** 32 + 4, 0), (4, 2 ** 32), (-2 ** 32 + 4, 0)])
+def test_window_that_no_int32_holds(lib, window, sinks):
+    """Refused by the binding: the library would get its low bits."""
+    import dual_ar_tts_frame_gb300 as D
+
+    class Handle:
+        calls = []
+        h = None
+
+        class lib:
+            dualar_set_attn_window = staticmethod(lambda *a: Handle.calls.append(a) or 0)
+
+        def _check(self, rc):
+            assert rc == 0
+
+    with pytest.raises(L.DualARError):
+        D.DualARDecoder.set_attn_window(Handle(), window, sinks)
+    D.DualARDecoder.set_attn_window(Handle(), 5, 2)
+    assert Handle.calls == [(None, 5, 2)]
