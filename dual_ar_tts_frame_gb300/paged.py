@@ -289,9 +289,11 @@ def paged_attention_workspace(q: torch.Tensor, kv: torch.Tensor, n_seq: int) -> 
 
 
 def check_errors(err: torch.Tensor) -> None:
-    """Synchronises with the work that reports into err, raises DualARError
-    (DUALAR_ERR_DEVICE) if a bounds check failed on the device or a wait there
-    ran out, and clears it."""
+    """Synchronises with err's device (the calls that report into err may be queued
+    on any stream), raises DualARError (DUALAR_ERR_DEVICE) if a bounds check failed
+    there or a wait ran out, and clears it."""
+    if err.is_cuda:
+        torch.cuda.synchronize(err.device)
     word = int(err.item())
     if word:
         err.zero_()

@@ -178,3 +178,21 @@ def test_a_wait_that_runs_out_leaves_no_wrong_rows(gen, shim, bits, act):
             assert int(err.item()) == 1 and torch.isnan(out[:sum(new)]).all()
         else:
             assert int(err.item()) == 0 and torch.equal(out[:sum(new)], want[:sum(new)])
+
+
+def test_errors_of_another_stream_are_waited_for(gen):
+    """check_errors on the default stream, while the call that reports is still
+    queued behind other work on a stream of its own."""
+    from dual_ar_tts_frame_gb300 import check_errors, kv_read
+    from dual_ar_tts_frame_gb300._lib import DualARError
+    kv = R.random_layer(2, 2, 64, 16, gen)[:, 0]
+    slot, err, side = i32([128]), i32([0]), torch.cuda.Stream()
+    kv_read(kv, i32([0]))
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(10 ** 8)
+        kv_read(kv, slot, err=err)
+    with pytest.raises(DualARError, match="slot"):
+        check_errors(err)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0
