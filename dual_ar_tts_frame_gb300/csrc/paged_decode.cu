@@ -30,9 +30,11 @@
 // take three shifts, four ORs and four subtractions.  The place is made up for by
 // the query (keys) or when an output row is added (values); the 8 is taken off
 // in the accumulator's initial value, -8 times the sum of what multiplies the
-// codes (fp32 activations: off the codes, one more instruction per register,
-// since those larger sums cost a truncating accumulator four times the error:
-// 4.4e-6 instead of 0.7e-6); and the token's scale multiplies its score or its
+// codes.  fp32 activations take q itself, 1024 + u less 1032, one more instruction
+// per register: with u the larger sums cost a truncating accumulator accuracy, and the
+// tensor cores align a subnormal operand's product by the exponent that it does not
+// have, which left 18 bits of a query beside a code of 1 (one request of 32K, error:
+// 4.4e-6 with u, 6.9e-7 with q as subnormals, 1.3e-7).  The token's scale multiplies its score or its
 // weight, never an element.  Queries are scaled by a power of two to their row's largest element,
 // weights to their chunk's, which keeps them inside fp16's range.  Any order of
 // the head's dimensions serves in the first product as long as the query uses it
@@ -176,18 +178,19 @@ DEVI void split_parts(float x, float y, uint32_t (&h)[N]) {
 }
 
 // 8 codes -> fp16 pairs of codes (j, j + 4), j = 0..3: u 2^-24 for even j, u 2^-20
-// for odd j; SIGNED: q instead of u (exact).
+// for odd j; SIGNED: q and 16 q, as normal numbers (exact: 1024 + u less 1032).
 template <bool SIGNED>
 DEVI void codes_f16(uint32_t w, uint32_t (&r)[4]) {
-  r[0] = w & 0x000F000Fu;
-  r[1] = w & 0x00F000F0u;
+  constexpr uint32_t one = SIGNED ? 0x64006400u : 0u;
+  r[0] = (w & 0x000F000Fu) | one;
+  r[1] = (w & 0x00F000F0u) | one;
   const uint32_t v = w >> 8;
-  r[2] = v & 0x000F000Fu;
-  r[3] = v & 0x00F000F0u;
+  r[2] = (v & 0x000F000Fu) | one;
+  r[3] = (v & 0x00F000F0u) | one;
   if constexpr (SIGNED) {
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r[j]) : "r"(r[j]), "r"(j & 1 ? 0x00800080u : 0x00080008u));
+      asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r[j]) : "r"(r[j]), "r"(j & 1 ? 0x64806480u : 0x64086408u));
   }
 }
 
@@ -468,7 +471,7 @@ __global__ void __launch_bounds__(Dec<HD, BITS, F32>::WARPS * 32, Dec<HD, BITS, 
             }
           sum += __shfl_xor_sync(0xffffffffu, sum, 1);
           sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-          const float qs = finite ? scalbnf(sc2, 24 - k) : NAN;
+          const float qs = finite ? scalbnf(sc2, (F32 ? 0 : 24) - k) : NAN;
 #pragma unroll
           for (int r2 = 0; r2 < 2; ++r2) {
             qinit[r2] = F32 ? 0.f : -0x1p-21f * __shfl_sync(0xffffffffu, sum, (2 * c + r2) * 4);
@@ -653,7 +656,7 @@ __global__ void __launch_bounds__(Dec<HD, BITS, F32>::WARPS * 32, Dec<HD, BITS, 
         for (int r = 0; r < 2; ++r) {
           const int ce = max(static_cast<int>(__float_as_uint(cm[r]) >> 23), 30);
           up[r] = pow2_biased(254 + 13 - ce);
-          f0[r] = cm[r] <= FLT_MAX ? pow2_biased(ce) : NAN;
+          f0[r] = cm[r] <= FLT_MAX ? pow2_biased(F32 ? ce - 13 : ce) : NAN;
           f1[r] = f0[r] * 0.0625f;
         }
         // and 8 times their sum, by a row of codes 8
@@ -739,7 +742,7 @@ __global__ void __launch_bounds__(Dec<HD, BITS, F32>::WARPS * 32, Dec<HD, BITS, 
         for (int r = 0; r < 2; ++r) {
           const int lr = 2 * c + r;
           const float inv = l[r] != 0.f ? 1.f / l[r] : 0.f;
-          const float unit = Q4 ? 0x1p11f : 1.f;   // 2^24 (codes) / 2^13 (weights)
+          const float unit = Q4 && !F32 ? 0x1p11f : 1.f;   // 2^24 (codes) / 2^13 (weights)
           const int64_t at = out_at(a, group, HD, ck.q0, r0 + lr, ck.head);
           const bool live = lr < nr;
           if constexpr (Q4) {
