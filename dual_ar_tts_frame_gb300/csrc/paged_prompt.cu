@@ -7,7 +7,7 @@
 // blocks of BT tokens: 128, or 64 (fp32: the weights' three parts lie over their
 // scores, and two score regions and O have to fit the 512 columns of TMEM).  Per block and tile
 //   S = Q K^T        tcgen05.mma, both operands in shared memory, S in TMEM
-//   P = exp2(S - m)  one thread per row reads S, writes P over it (bf16)
+//   P = exp2(S - m)  one thread per row reads S, writes P over it (in bf16 parts)
 //   O += P V         tcgen05.mma, P from TMEM, V^T straight from V's rows (MN-major)
 // Roles: 4 warps per tile for the rows (fp32: 16 warps, four threads per row), 1
 // thread issues MMAs, 3 to 7 warps load.  While one tile's rows are worked on, the
@@ -18,6 +18,11 @@
 // fp32 activations: query and weights as three bf16 parts each (24 bits), their
 // products added in the accumulator; every block's O leaves the accumulator,
 // which truncates, and is added in registers with rounding.
+//
+// bf16 activations: the query is exact, a weight has two bf16 parts (16 bits).  With
+// one, the rounding of the weights is as large as the output's own (four windowed
+// prompts, error against 64 bits: 2.1e-3 instead of 1.6e-3, at 219 us instead of 248),
+// and a row's precision would depend on how many rows its request has.
 //
 // A 4-bit cache is widened by the loading warps to bf16 integers q (exact); the
 // token's scale multiplies its score or its weight.
@@ -60,7 +65,8 @@ constexpr float kLazyMax = 8.f;                     // a row's maximum may lag b
 template <int HD, int BITS, bool F32>
 struct Pro {
   static constexpr int NT = F32 ? 1 : 2;             // tiles of 128 rows
-  static constexpr int NP = F32 ? 3 : 1;             // bf16 parts of a query element and of a weight
+  static constexpr int NP = F32 ? 3 : 1;             // bf16 parts of a query element
+  static constexpr int PP = F32 ? 3 : 2;             // and of a weight
   static constexpr int BT = F32 ? 64 : 128;          // tokens per block
   static constexpr int TILE = 128 * NT;
   static constexpr int SUBS = HD / 64;               // 128-byte wide sub-tiles of an operand row
@@ -79,7 +85,11 @@ struct Pro {
   static constexpr int NSLOT = ROOM / SLOT > 8 ? 8 : ROOM / SLOT;
   static constexpr int THREADS = ROWS + 32 + LOAD;
   static constexpr int PCOLS = BT / 2;               // TMEM columns of one part of the weights
-  static constexpr int SCOLS = NP * PCOLS > BT ? NP * PCOLS : BT;   // of a tile's scores, or weights over them
+  static constexpr int SCOLS = PP * PCOLS > BT ? PP * PCOLS : BT;   // of a tile's scores, or weights over them
+  // Column of part q of the weights of 16 tokens from 16 k.  bf16 rows read their scores
+  // in chunks of 32 columns (32 tokens) and put both parts of those weights over each;
+  // fp32 rows hold theirs by then, and the parts lie one after the other.
+  static constexpr int weight_col(int q, int k) { return F32 ? q * PCOLS + k * 8 : (k >> 1) * 32 + q * 16 + (k & 1) * 8; }
   static constexpr int RB = F32 ? 2 : 1;             // score regions of a tile
   static constexpr int TCOLS = RB * SCOLS + HD;      // of a tile
   static constexpr uint32_t ALLOC = NT * TCOLS <= 256 ? 256 : 512;
@@ -200,7 +210,7 @@ __global__ void __launch_bounds__(Pro<HD, BITS, F32>::THREADS, 1)
     attn_prompt_kernel(const __grid_constant__ CUtensorMap tkv, const __grid_constant__ CUtensorMap tq, const AttnArgs a,
                        const int use_tma) {
   using D = Pro<HD, BITS, F32>;
-  constexpr int NT = D::NT, NP = D::NP, BT = D::BT, TILE = D::TILE, NSLOT = D::NSLOT, LT = D::LOAD, RB = D::RB, H = D::H;
+  constexpr int NT = D::NT, NP = D::NP, PP = D::PP, BT = D::BT, TILE = D::TILE, NSLOT = D::NSLOT, LT = D::LOAD, RB = D::RB, H = D::H;
   constexpr bool Q4 = BITS == 4;
   using Walk = AttnWalk<TILE, BT>;
   extern __shared__ unsigned char smem_raw[];
@@ -513,11 +523,11 @@ __global__ void __launch_bounds__(Pro<HD, BITS, F32>::THREADS, 1)
         const uint32_t td = tm + t * D::TCOLS + (b % RB) * D::SCOLS, to = tm + t * D::TCOLS + RB * D::SCOLS;
         const uint64_t vd = smem_desc_mn_sw128(ring_a + ((2 * b + 1) % NSLOT) * D::SLOT, BT * 128);
 #pragma unroll
-        for (int p = NP - 1; p >= 0; --p)
+        for (int p = PP - 1; p >= 0; --p)
 #pragma unroll
           for (int k = 0; k < BT / 16; ++k)
-            tc_mma_ts(to, td + p * D::PCOLS + k * 8, vd + ((k * 2048) >> 4), id_o,
-                      p < NP - 1 || k > 0 || (!first && !F32));
+            tc_mma_ts(to, td + D::weight_col(p, k), vd + ((k * 2048) >> 4), id_o,
+                      p < PP - 1 || k > 0 || (!first && !F32));
       };
       auto wait = [&](uint64_t* bar, int phase) {
         if (dead) return;
@@ -780,18 +790,18 @@ __global__ void __launch_bounds__(Pro<HD, BITS, F32>::THREADS, 1)
           }
         }
 #pragma unroll
-        for (int q = 0; q < NP; ++q) {
+        for (int q = 0; q < PP; ++q) {
           uint32_t w[CW / 2];
 #pragma unroll
           for (int i = 0; i < CW / 2; ++i) {
             w[i] = pack_bf16(x[2 * i], x[2 * i + 1]);
-            if (q + 1 < NP) {
+            if (q + 1 < PP) {
               x[2 * i] -= bf16lo(w[i]);
               x[2 * i + 1] -= bf16hi(w[i]);
             }
           }
-          if constexpr (CW == 32) tmem_st16(ts + q * D::PCOLS + ch * 16, w);
-          else tmem_st8(ts + q * D::PCOLS + ch * 8, w);
+          if constexpr (CW == 32) tmem_st16(ts + D::weight_col(q, 2 * ch), w);
+          else tmem_st8(ts + D::weight_col(q, ch), w);
         }
       }
       l = fmaf(l, f, lb);

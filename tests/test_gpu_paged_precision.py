@@ -96,7 +96,7 @@ KEPT = {(torch.float32, 16, "few"): 24, (torch.float32, 4, "few"): 22, (torch.fl
 
 
 @pytest.mark.parametrize("bits", [16, 4])
-@pytest.mark.parametrize("act,off", [(torch.float32, 2)])
+@pytest.mark.parametrize("act,off", [(torch.float32, 2), (torch.bfloat16, 1)])
 def test_bits_of_a_weight(bits, act, off):
     s, w, parts, left = weight_with(off, 0.9 * 2.0 ** (-10 if off == 1 else -19))
     keys = [{}] * off + [{0: -1.0}]
