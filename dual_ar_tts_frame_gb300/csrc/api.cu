@@ -22,7 +22,7 @@
 namespace dualar {
 // (weak: a build of this file alone has no windowed attention)
 __attribute__((weak)) cudaError_t launch_decoder_step(const DevPtrs&, int, bool, const StepBuffers&, cudaStream_t);
-__attribute__((weak)) cudaError_t launch_qk_norm_rope(const NormRopeArgs&, bool, int, cudaStream_t);
+__attribute__((weak)) cudaError_t launch_qk_norm_rope(const NormRopeArgs&, bool, cudaStream_t);
 __attribute__((weak)) cudaError_t launch_paged_attention(const AttnArgs&, bool, int, cudaStream_t);
 __attribute__((weak)) int64_t paged_attention_workspace(bool, int, int, int, int, int, int);
 }  // namespace dualar
@@ -488,7 +488,7 @@ int block(dualar_handle* h, const dualar_layer_weights& lw, int layer, bool fast
     const int64_t qd = static_cast<int64_t>(c.n_head) * c.head_dim;
     LAUNCH(h, launch_qk_norm_rope(NormRopeArgs{d.qkv, d.qkv_dim, nrows, c.n_head, kv, h->step.pos, h->step.slot, qn, kn,
                                                c.norm_eps, d.rope_cos, d.rope_sin, d.rope_len, d.qrot, qd, d.err},
-                                  false, h->n_sm, h->stream));
+                                  false, h->stream));
     LAUNCH(h, launch_paged_attention(
                   AttnArgs{d.qrot, qd, nrows, c.n_head, kv, d.page_table, d.pages_per_seq, h->step.table_row,
                            h->step.row_start, h->step.kv_len, fuse_append ? nrows : 1, h->window, h->sinks,

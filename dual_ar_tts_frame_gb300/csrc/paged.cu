@@ -402,8 +402,7 @@ static cudaError_t norm_rope_one(const NormRopeArgs& a, cudaStream_t st) {
                     st, a);
 }
 
-cudaError_t launch_qk_norm_rope(const NormRopeArgs& a, bool bf16, int n_sm, cudaStream_t st) {
-  (void)n_sm;
+cudaError_t launch_qk_norm_rope(const NormRopeArgs& a, bool bf16, cudaStream_t st) {
   if (a.kv.head_dim == 128) return bf16 ? norm_rope_one<true, 128>(a, st) : norm_rope_one<false, 128>(a, st);
   return bf16 ? norm_rope_one<true, 64>(a, st) : norm_rope_one<false, 64>(a, st);
 }

@@ -11,7 +11,7 @@ namespace dualar {
 constexpr int kPageTokens = 64;
 constexpr int kMaxPlanSeqs = 8192;      // requests of a call
 constexpr int kMaxTableWidth = 1 << 20;  // pages per request
-constexpr int kAttnSms = 152;            // multiprocessors that the attention kernels use at most
+constexpr int kAttnSms = 152;            // multiprocessors that the attention kernels use at most: GB300's, which workspaces are sized for
 
 struct KvView {
   unsigned char* data;
@@ -49,7 +49,7 @@ struct NormRopeArgs {
   int64_t ldq;
   uint32_t* err;
 };
-cudaError_t launch_qk_norm_rope(const NormRopeArgs& a, bool bf16, int n_sm, cudaStream_t st);
+cudaError_t launch_qk_norm_rope(const NormRopeArgs& a, bool bf16, cudaStream_t st);
 
 cudaError_t launch_kv_read(const KvView& kv, const int32_t* slot, int n, float* k, float* v, uint32_t* err,
                            cudaStream_t st);

@@ -132,9 +132,7 @@ int dualar_qk_norm_rope(const void* qkv, int32_t act, int64_t ld, int32_t rows, 
   a.q_out = q_out;
   a.ldq = ldq;
   a.err = dev_error;
-  int n_sm = 0;
-  if (const int rc = sm_count(&n_sm)) return rc;
-  return done("qk_norm_rope", launch_qk_norm_rope(a, act == DUALAR_BF16, n_sm, static_cast<cudaStream_t>(cuda_stream)));
+  return done("qk_norm_rope", launch_qk_norm_rope(a, act == DUALAR_BF16, static_cast<cudaStream_t>(cuda_stream)));
 }
 
 int dualar_kv_read(const dualar_kv* kv, const int32_t* slot, int32_t n, float* k, float* v, uint32_t* dev_error,

@@ -154,11 +154,6 @@ DEVI void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
   tmem_ld16_async(taddr, lo);
   tmem_ld16_async(taddr + 16, hi);
 }
-DEVI float pro_exp2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 DEVI void tma_load_3d(uint32_t dst, const void* tmap, int x, int y, int z, uint64_t* bar) {
   asm volatile(
       "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
@@ -173,13 +168,6 @@ DEVI void tma_load_4d(uint32_t dst, const void* tmap, int x, int y, int z, int w
       : "memory");
 }
 DEVI void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-DEVI void cp16z(uint32_t dst, const void* src, bool take) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(take ? 16 : 0) : "memory");
-}
-template <int N>
-DEVI void cp_wait_group() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 
 // 8 codes as 8 bf16 integers q.
 DEVI uint4 widen_codes(uint32_t w) {
@@ -389,10 +377,10 @@ __global__ void __launch_bounds__(Pro<HD, BITS, F32>::THREADS, 1)
           for (int id = t; id < TILE * PR; id += LT) {
             const int row = id / PR, c8 = id % PR;
             const bool live = row < wk.u.nr;
-            cp16z(q_place(row, c8), static_cast<const uint16_t*>(a.q) + (live ? q_source(rows, row, c8) : 0), live);
+            cp16_or_zero(q_place(row, c8), static_cast<const uint16_t*>(a.q) + (live ? q_source(rows, row, c8) : 0), live);
           }
           cp_async_commit();
-          cp_wait_group<0>();
+          cp_wait<0>();
           fence_async_smem();
           mbar_arrive(&qfull);
         }
@@ -453,11 +441,11 @@ __global__ void __launch_bounds__(Pro<HD, BITS, F32>::THREADS, 1)
 #pragma unroll 4
             for (int id = t; id < BT * PC; id += LT) {
               const int tok = id / PC, c = id % PC;
-              cp16z(dst + (c >> 3) * (BT * 128) + tok * 128 + (((c & 7) ^ (tok & 7)) << 4),
+              cp16_or_zero(dst + (c >> 3) * (BT * 128) + tok * 128 + (((c & 7) ^ (tok & 7)) << 4),
                     kv_block(a.kv, BT > 64 && tok >= 64 ? k.page1 : k.page0, kv, k.head) + (tok & 63) * (HD * 2) + c * 16, take(tok));
             }
             cp_async_commit();
-            cp_wait_group<0>();
+            cp_wait<0>();
             publish(slot);
           }
         } else {
@@ -750,7 +738,7 @@ __global__ void __launch_bounds__(Pro<HD, BITS, F32>::THREADS, 1)
       mx = mx > -FLT_MAX ? mx * sc2 : -FLT_MAX;
       const bool grow = mx > m + kLazyMax || m == -FLT_MAX;
       const float mn = grow ? fmaxf(mx, m) : m;
-      const float f = pro_exp2(m - mn);
+      const float f = exp2_fast(m - mn);
       if constexpr (!F32) {
         if (__any_sync(0xffffffffu, grow && l > 0.f)) {
 #pragma unroll 1
@@ -775,7 +763,7 @@ __global__ void __launch_bounds__(Pro<HD, BITS, F32>::THREADS, 1)
         float l4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int i = 0; i < CW; ++i) {
-          x[i] = pro_exp2(fmaf(x[i], sc2, -m));
+          x[i] = exp2_fast(fmaf(x[i], sc2, -m));
           l4[i & 3] += x[i];
         }
         lb += (l4[0] + l4[1]) + (l4[2] + l4[3]);
