@@ -19,9 +19,10 @@
 // Precision.  bf16 cache: bf16 parts of the other factor, multiplied one after
 // the other into one accumulator: fp32 activations 3 (24 bits of query and
 // weight), bf16 activations 1 of the query (exact) and 2 of the weight.
-// 4-bit cache: fp16 parts, fp32 activations 2 (22 bits), bf16 activations 1 of the
-// query (exact) and 1 of the weight (11 bits, three more than the output's; with 2 the
-// error against 64 bits is the same 1.7e-3, and 161 us become 172).  The tensor cores' accumulators truncate (measured);
+// 4-bit cache: fp16 parts, 2 of the weight (22 bits) and of an fp32 query, 1 of a bf16
+// query (exact).  (With 1 part of the weight, 11 bits, bf16 rows take 161 us instead of
+// 172 for 64 requests; the error of typical rows is the output's rounding either way,
+// that of rows whose values cancel is not.)  The tensor cores' accumulators truncate (measured);
 // for fp32 activations and the 4-bit cache a chunk's sums leave them and are
 // added to the running output with rounding.
 //
@@ -79,7 +80,7 @@ struct Dec {
   static constexpr int SMEM = WARPS * (RING + PART * 4);
   static constexpr int KS = HD / 16;                             // k steps of the first product
   static constexpr int QP = F32 ? (BITS == 4 ? 2 : 3) : 1;       // parts of a query element
-  static constexpr int PP = BITS == 4 ? (F32 ? 2 : 1) : (F32 ? 3 : 2);   // parts of a weight
+  static constexpr int PP = BITS == 4 || !F32 ? 2 : 3;   // parts of a weight
   static constexpr bool OWN = BITS == 4 || F32;                  // a chunk has its own accumulators
 };
 

@@ -153,8 +153,7 @@ int64_t dualar_paged_attention_workspace(int32_t act, int32_t rows, int32_t n_he
  * value that one row of a request sees may reach its other rows of the call.
  * Sums and softmax statistics are fp32.  fp32 activations: queries and weights
  * keep 22 significant bits at least.  bf16: queries are taken as they are, weights
- * keep 16 bits at least (over 4 bits, where requests have few rows: 11, of the
- * weight times the value's scale).
+ * keep 16 bits at least.
  * The result depends on the arguments and the device alone, not on timing; but
  * for waits inside the kernels, which end after 2 s (a device taken from the call
  * meanwhile): every row of the call is then NaN and *dev_error has

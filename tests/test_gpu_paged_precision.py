@@ -87,11 +87,10 @@ def weight_with(bits_off, at_least):
             return s, w, parts, left
 
 
-# what a weight may be off by itself: fp32 rows keep three bf16 parts (24 bits; two of
-# fp16, 22 bits, over 4 bits and few rows), bf16 rows two (16 bits; one of fp16, 11 bits,
-# over 4 bits and few rows)
+# what a weight may be off by itself: fp32 rows keep three bf16 parts (24 bits), bf16 rows
+# two (16 bits); over 4 bits few rows keep two fp16 parts (22 bits)
 KEPT = {(torch.float32, 16, "few"): 24, (torch.float32, 4, "few"): 22, (torch.float32, 16, "many"): 24,
-        (torch.float32, 4, "many"): 24, (torch.bfloat16, 16, "few"): 16, (torch.bfloat16, 4, "few"): 11,
+        (torch.float32, 4, "many"): 24, (torch.bfloat16, 16, "few"): 16, (torch.bfloat16, 4, "few"): 22,
         (torch.bfloat16, 16, "many"): 16, (torch.bfloat16, 4, "many"): 16}
 
 
@@ -110,9 +109,16 @@ def test_bits_of_a_weight(bits, act, off):
         # of two the step is 2^(1 - n) of it)
         kept = 2.0 ** -KEPT[act, bits, kernel]
         tol = w * (kept + REST) / (off + w) + exact * torch.finfo(act).eps / 2
+        other = 0.0                                         # of elements that are zero in all values
+        if act == torch.bfloat16 and bits == 4 and kernel == "few":
+            # sums over u = q + 8 that start at -8 times the weights' sum: 8 additions for
+            # the start and at most 8 for the codes, of terms up to 15 w_j s_j (s_j the value's
+            # scale), each truncated at 2^-23 of its size: 16 * 15 * 2^-23 < 2^-15 of sum w_j s_j
+            other = 2.0 ** -15 * (sum(parts) + w) / (off + w)
+            tol += other
         err = (got[:, 5] - exact).abs().max().item()
         assert err <= tol, (kernel, err, tol, exact)
-        assert (got[:, :5] == 0).all() and (got[:, 6:] == 0).all()
+        assert max(got[:, :5].abs().max().item(), got[:, 6:].abs().max().item()) <= other
 
 
 @pytest.mark.parametrize("bits", [16, 4])
