@@ -493,12 +493,17 @@ cudaError_t launch_decoder_step(const DevPtrs& d, int nrows, bool one_sequence, 
 // Few (token, head) rows a request on average: the decode kernel.  Both kernels are
 // right for any rows; the decode kernel reads a request's cache once per 8 rows, the
 // other once per 128 or 256 and pads its tiles to that.  The limits are where the two
-// cross: 32 requests of 4000 tokens, 8 heads of 128, us per call (decode kernel, other):
+// cross for requests of equal rows: 32 of 4000 tokens, 8 heads of 128, us per call
+// (decode kernel, other):
 //   rows           8          16         24         32         64
-//   bf16         91, 138   116, 138   240, 139   214, 139   410, 141
-//   bf16, fp32   94, 216   142, 216   245, 217   268, 217   516, 217
-//   4 bits       51, 197    82, 198   114, 198   144, 198   271, 200
-//   4 bits, fp32 75, 263   124, 264   185, 264   222, 265   423, 266
+//   bf16         89, 178   116, 180   234, 179   214, 180   411, 181
+//   bf16, fp32   93, 220   143, 221   237, 221   269, 221   516, 220
+//   4 bits       53, 226    86, 227   121, 226   154, 227   290, 228
+//   4 bits, fp32 76, 262   126, 262   187, 262   226, 263   432, 264
+// One kernel serves the whole call, which costs mixed steps: 500 single tokens beside a
+// chunk of 1500 (bf16: 698 and 248 us apart, 2616 together; 64 beside it: 63, 248 and
+// 367), and rows are the call's, so those behind the last request count: 64 single
+// tokens padded to 1024 rows take 228 us instead of 110 (to 128 rows: 110).
 static bool few_rows(int bits, int rows, int group, int n_seq) {
   return static_cast<long long>(rows) * group <= (bits == 4 ? 32ll : 16ll) * n_seq;
 }

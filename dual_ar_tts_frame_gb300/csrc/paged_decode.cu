@@ -44,10 +44,12 @@
 // one contiguous vector, and its outputs are contiguous.
 //
 // Measured (32 query and 8 key/value heads of 128):
-//   bf16 cache, 64 requests, window 1024 + 4 first tokens: 53 us, 5.1 TB/s, 75% of a
+//   bf16 cache, 64 requests, window 1024 + 4 first tokens: 54 us, 5.0 TB/s, 74% of a
 //     copy's rate; bound by memory, and by the start and the join of a short kernel.
-//   4 bits, 64 requests of 2000 to 16384 tokens: 160 us, 3.9 TB/s, 57%; bound by
-//     instruction issue: 108 M of them, 178,000 per scheduler, for 620 MB.
+//   4 bits, 64 requests of 2000 to 16384 tokens, bf16 rows: 170 us, 3.7 TB/s, 54%.  59% of
+//     issue slots are in use, with four warps per scheduler: a chunk is one dependent
+//     chain (scores, maximum, exponentials, the weights' scale, values), and nothing of
+//     a warp's next chunk runs beside it.
 //   4 bits, one request of 32K: 28 us; 304 CTAs, of which each has 7 chunks per warp:
 //     the start (work shares, first loads) and the join are most of it.
 #include <cfloat>

@@ -31,19 +31,21 @@
 // lengths are; units that fall on two CTAs are joined by attn_join_kernel.
 //
 // Measured (32 query and 8 key/value heads of 128):
-//   bf16, four prompts with a window: 207 us, 425 TFLOP/s of the seen pairs.  A block
-//     of 2 x 128 rows x 128 tokens takes 2.2 us: by timestamps, a tile's rows work 1.1
-//     us and 1.1 pass from its weights to its next scores, while the rows of the other
-//     tile work.  The 16 MMAs between are 0.5 us by themselves; the rest is latency of
-//     their issue and completion.  Two threads per row do not shorten it (229 us per
-//     call instead of 215).  What a window masks in a block is multiplied all the same.
-//   bf16, two prompts without a window: 154 us, 810 TFLOP/s.
-//   fp32 over 4 bits, the same prompts: 461 us, 270 TFLOP/s, three times that in MMAs:
-//     each is done for three parts.  A block of 64 tokens takes 1.9 us, all of it on the
-//     MMA thread; its 36 MMAs run in 1.05 alone, the scores' at the rate at which
-//     shared memory gives the query.
-//   fp32 over bf16: 438 us.
-// fp32 rows took 700 us with two threads per row, whose queries the loaders brought in
+//   bf16, four prompts with a window: 239 us, 368 TFLOP/s of the seen pairs; two without
+//     a window: 192 us, 650 TFLOP/s.  The windowed ones have fewer blocks per CTA (45
+//     against 51) but more that are partial (11.6 against 2.1: copied by the threads, one
+//     slot at a time) and more units (5 against 2.5: the next unit's scores wait for all
+//     values of the last).  With one part per weight a block of 2 x 128 rows x 128 tokens
+//     took 2.2 us, by timestamps: a tile's rows work 1.1 us, in which they read the scores
+//     from TMEM twice, a chunk at a time, and 1.1 pass from its weights to its next
+//     scores, while the rows of the other tile work; the 16 MMAs between are 0.5 us by
+//     themselves.  The second part costs 14 us of MMAs and 20 of the rows (192 us).
+//   fp32 over 4 bits, two prompts: 470 us, 264 TFLOP/s, three times that in MMAs: each is
+//     done for three parts.  A block of 64 tokens takes 1.9 us, all of it on the MMA
+//     thread; its 36 MMAs run in 1.05 alone, the scores' at the rate at which shared
+//     memory gives the query.
+//   fp32 over bf16: 443 us.
+// fp32 rows over 4 bits took 700 us with two threads per row, whose queries the loaders brought in
 // between two units and whose MMA thread walked the work line itself.
 #include <cfloat>
 #include <cuda.h>

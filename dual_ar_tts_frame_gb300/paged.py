@@ -238,8 +238,8 @@ def paged_attention(q: torch.Tensor, kv: torch.Tensor, table: torch.Tensor, row_
     positions each row sees.  kv_len [n_seq] counts the new tokens (KVPlan.new_len);
     table [n_seq, width]; row_start [n_seq + 1].  window 0: every position up to
     the row's own; else the last `window` of them and the first `sinks`.  scale:
-    head_dim^-0.5 by default.  Rows behind the last request are left as they are
-    in `out` (undefined where it is allocated here).  workspace: by default one
+    head_dim^-0.5 by default.  Rows before the first request and behind the last are
+    left as they are in `out` (undefined where it is allocated here).  workspace: by default one
     that the call allocates; a given one belongs to one call at a time."""
     c, dev, lib = _kv(kv), kv.get_device(), L.lib()
     d = c.head_dim

@@ -366,7 +366,11 @@ int dualar_set_tensor_cores(dualar_handle* h, int32_t enable);
  * longer grows with it.  window 0 (default): every position.  The fast AR and the
  * cache, which keeps every position, are unaffected.  While a window is set,
  * prefill and decode run one kernel per op for every batch, with the operators of
- * dualar_paged.h as the slow attention.  The first call with a window allocates
+ * dualar_paged.h as the slow attention.  At the S2-Pro shape on GB300 a frame with
+ * window 1024 and 64 sinks takes 4.5 ms at batch 1 and 5.9 at batch 2 (without a
+ * window 3.8 and 5.7 at 1024 positions, 4.5 and 7.1 at 4096, 6.2 and 10.4 at 16384),
+ * 6.0 at batch 16 and 7.7 at batch 64 (7.2 and 11.5 at 4096 positions); a prefill
+ * of 8192 positions 268 ms instead of 542.  The first call with a window allocates
  * its workspace.  The pages know no such window.  Errors: INVALID_ARG (negative),
  * CUDA (no memory). */
 int dualar_set_attn_window(dualar_handle* h, int32_t window, int32_t sinks);

@@ -148,7 +148,7 @@ int64_t dualar_paged_attention_workspace(int32_t act, int32_t rows, int32_t n_he
  *   q, out: act [rows][ld], n_head heads of head_dim; 16-byte aligned rows
  *   table:  [n_seq][table_width] page numbers; entries that no row sees are not
  *           read as pages (a page that left the window may be reused)
- * Rows behind row_start[n_seq] are left as they were.  What cached positions that
+ * Rows before row_start[0] and behind row_start[n_seq] are left as they were.  What cached positions that
  * no row of the call sees hold (infinities, NaN) has no effect; a non-finite
  * value that one row of a request sees may reach its other rows of the call.
  * Sums and softmax statistics are fp32.  fp32 activations: queries and weights
@@ -158,6 +158,11 @@ int64_t dualar_paged_attention_workspace(int32_t act, int32_t rows, int32_t n_he
  * for waits inside the kernels, which end after 2 s (a device taken from the call
  * meanwhile): every row of the call is then NaN and *dev_error has
  * DUALAR_PAGED_ERR_WAIT.
+ * One of two kernels serves the whole call, chosen by rows / n_seq: few rows per
+ * request, or many (padding counts).  Where a long prompt comes beside many single
+ * tokens, two calls can take a fraction of the time: one for the requests of single
+ * tokens, which come first (their rows and n_seq), one for the others (row_start,
+ * kv_len and table from their first request on, the same q, out and rows).
  * n_head / n_kv_head <= 32, rows <= 2^24, table_width <= 2^20, n_seq <= 8192;
  * workspace: dualar_paged_attention_workspace bytes, 16-byte aligned, any
  * contents. */

@@ -107,6 +107,28 @@ def test_a_plan_into_a_page_out_of_range_is_refused(n, page):
     assert p.status.tolist() == [0, 3 * n, 1] and p.slot[3 * n - 3:3 * n].tolist() == [3 * n * 64 + i for i in range(3)]
 
 
+@pytest.mark.parametrize("bits", [16, 4])
+@pytest.mark.parametrize("act", [torch.float32, torch.bfloat16])
+def test_a_mixed_step_in_one_call_and_in_two(gen, bits, act):
+    """Many single tokens beside a chunk of a prompt: in one call (whichever kernel
+    that takes), and the single tokens in one, the chunk in another over the same
+    tensors, which leaves the first one's rows alone."""
+    from dual_ar_tts_frame_gb300 import paged_attention
+    singles, h, hk, d = 70, 8, 2, 128
+    new, ctx = [1] * singles + [400, 33], [1 + 9 * i for i in range(singles)] + [900, 33]
+    n_pages = sum(-(-c // PAGE) for c in ctx) + 1
+    kv = R.random_layer(n_pages, hk, d, bits, gen)[:, 0]
+    table, start, lens = R.layout(new, ctx, n_pages)
+    q = torch.randn((sum(new), h, d), generator=gen, device="cuda").to(act)
+    for window, sinks in ((0, 0), (100, 3)):
+        R.assert_attention(paged_attention(q, kv, table, start, lens, window, sinks), q, kv, table, start, lens, window, sinks)
+        out = torch.full_like(q, 7.0)
+        paged_attention(q, kv, table[singles:], start[singles:], lens[singles:], window, sinks, out=out)
+        assert (out[:singles] == 7).all()
+        paged_attention(q[:singles], kv, table[:singles], start[:singles + 1], lens[:singles], window, sinks, out=out[:singles])
+        R.assert_attention(out, q, kv, table, start, lens, window, sinks)
+
+
 SHIM = r"""
 #include "paged.h"
 // The prompt kernel and its join; no_waiting: its waits run out at once.
