@@ -11,7 +11,7 @@ namespace dualar {
 constexpr int kPageTokens = 64;
 constexpr int kMaxPlanSeqs = 8192;      // requests of a call
 constexpr int kMaxTableWidth = 1 << 20;  // pages per request
-constexpr int kAttnSms = 152;            // multiprocessors that the attention kernels use at most: GB300's, which workspaces are sized for
+constexpr int kAttnSms = 152;            // multiprocessors that the attention kernels use at most (GB300's; workspaces fit them)
 
 struct KvView {
   unsigned char* data;

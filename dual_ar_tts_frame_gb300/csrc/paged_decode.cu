@@ -32,15 +32,17 @@
 // take three shifts, four ORs and four subtractions.  The place is made up for by
 // the query (keys) or when an output row is added (values); the 8 is taken off
 // in the accumulator's initial value, -8 times the sum of what multiplies the
-// codes.  fp32 activations take q itself, 1024 + u less 1032, one more instruction
-// per register: with u the larger sums cost a truncating accumulator accuracy, and the
-// tensor cores align a subnormal operand's product by the exponent that it does not
-// have, which left 18 bits of a query beside a code of 1 (one request of 32K, error:
-// 4.4e-6 with u, 6.9e-7 with q as subnormals, 1.3e-7).  The token's scale multiplies its score or its
-// weight, never an element.  Queries are scaled by a power of two to their row's largest element,
-// weights to their chunk's, which keeps them inside fp16's range.  Any order of
-// the head's dimensions serves in the first product as long as the query uses it
-// too, and any order of output rows in the second; so a lane reads its codes as
+// codes (the sums' terms are then up to 15 of a token's scale: at most 2^-15 of sum_j
+// w_j s_j of error, below the output's rounding of typical rows).  fp32 activations take
+// q itself, 1024 + u less 1032, one more instruction per register: with u the larger
+// sums cost a truncating accumulator accuracy, and the tensor cores align a subnormal
+// operand's product by the exponent that it does not have, which left 18 bits of a query
+// beside a code of 1 (one request of 32K, error: 4.4e-6 with u, 6.9e-7 with q as
+// subnormals, 1.3e-7).  The token's scale multiplies its score or its weight, never an
+// element.  Queries are scaled by a power of two to their row's largest element, weights
+// to their chunk's, which keeps them inside fp16's range.  Any order of the head's
+// dimensions serves in the first product as long as the query uses it too, and any order
+// of output rows in the second; so a lane reads its codes as
 // one contiguous vector, and its outputs are contiguous.
 //
 // Measured (32 query and 8 key/value heads of 128):
@@ -848,9 +850,9 @@ __global__ void __launch_bounds__(Dec<HD, BITS, F32>::WARPS * 32, Dec<HD, BITS, 
 // are right is not known.
 template <int HD, bool F32>
 __device__ __noinline__ void rows_are_lost(const AttnArgs& a) {
-  const int end = min(a.rows, a.row_start[a.n_seq]), width = a.n_head * HD;
+  const int begin = min(a.rows, max(0, a.row_start[0])), end = min(a.rows, a.row_start[a.n_seq]), width = a.n_head * HD;
   const float nan[2] = {NAN, NAN};
-  for (int row = max(0, a.row_start[0]) + blockIdx.y * gridDim.x + blockIdx.x; row < end; row += gridDim.x * gridDim.y)
+  for (int row = begin + blockIdx.y * gridDim.x + blockIdx.x; row < end; row += gridDim.x * gridDim.y)
     for (int i = threadIdx.x * 2; i < width; i += 512) store_act<!F32, 2>(a.out, static_cast<int64_t>(row) * a.ldo + i, nan);
 }
 

@@ -148,9 +148,10 @@ int64_t dualar_paged_attention_workspace(int32_t act, int32_t rows, int32_t n_he
  *   q, out: act [rows][ld], n_head heads of head_dim; 16-byte aligned rows
  *   table:  [n_seq][table_width] page numbers; entries that no row sees are not
  *           read as pages (a page that left the window may be reused)
- * Rows before row_start[0] and behind row_start[n_seq] are left as they were.  What cached positions that
- * no row of the call sees hold (infinities, NaN) has no effect; a non-finite
- * value that one row of a request sees may reach its other rows of the call.
+ * Rows before row_start[0] and behind row_start[n_seq] are left as they were.
+ * What cached positions that no row of the call sees hold (infinities, NaN) has no
+ * effect; a non-finite value that one row of a request sees may reach its other
+ * rows of the call.
  * Sums and softmax statistics are fp32.  fp32 activations: queries and weights
  * keep 22 significant bits at least.  bf16: queries are taken as they are, weights
  * keep 16 bits at least.
