@@ -1,7 +1,6 @@
 """The torch side of the paged key/value operators (paged.py) without a GPU:
 tensors in host memory that say they are on device 0, with the library's entry
 point replaced where a call would go on to the device."""
-import ctypes
 import gc
 import os
 import re
